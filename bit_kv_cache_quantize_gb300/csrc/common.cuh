@@ -7,6 +7,7 @@
 
 #include "params.h"
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 #include <type_traits>
 #include <cuda_fp16.h>
@@ -318,16 +319,12 @@ __device__ __forceinline__ void store4(O* dst, float4 o) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(f2bits<O>(o.x), f2bits<O>(o.y)), pack2(f2bits<O>(o.z), f2bits<O>(o.w)));
 }
 
-// Result of a row that no finite score reached (4 channels per lane): zeros, or
-// NaN where the query itself holds a value that is not finite, whose NaN scores
-// no running maximum keeps.
-__device__ __forceinline__ float4 unreached_row(const void* q, int64_t row, uint32_t exp16, int lane) {
-  const uint2 w = static_cast<const uint2*>(q)[row * (D / 4) + lane];
-  const uint32_t hi = exp16 << 16;
-  const bool bad = (w.x & exp16) == exp16 || (w.x & hi) == hi || (w.y & exp16) == exp16 || (w.y & hi) == hi;
-  const float r = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7FC00000) : 0.f;
-  return make_float4(r, r, r, r);
-}
+// Window and tree calls: the running maximum m of a row that has seen a token
+// is at least SEEN, so m = -inf says that the row has seen nothing (its result
+// is zeros), not that no score was a number.  fmaxf passes over NaN scores, and
+// -inf scores do not raise it: such rows keep m = SEEN with l = NaN or 0, which
+// merges carry on and whose quotient is NaN, as the formula's.
+constexpr float SEEN = -FLT_MAX;
 
 // x = x H over the 128 channels held 4 per lane.
 __device__ __forceinline__ void fwht128(float (&x)[4], int lane) {

@@ -135,7 +135,7 @@ template <typename E, int NW>
 __device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, const WinTiles& wt, unsigned char* smem,
                                float* part, int64_t part_stride);
 template <int NW, typename O>
-__device__ void win_cluster_merge(const DecodeParams& p, int b, int h, int len, const float* part, O* out);
+__device__ void win_cluster_merge(const DecodeParams& p, int b, int h, const float* part, O* out);
 
 // Unpacking codes to exact fp16 operands.  A code field ORed into the
 // mantissa of 1024.0 (0x6400) and 1024 subtracted gives the code exactly.
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(32 * NW, 2) decode_packed_kernel(DecodeParams 
     if constexpr (WIN == WIN_SPLIT) wait_prerequisite();  // the open tiles' kernel is complete when this grid is
     if constexpr (WIN == WIN_CLUSTER) {
       if (empty && tid < 8) cpart[tid][0] = -INFINITY;
-      win_cluster_merge<NW>(p, b, h, len, &cpart[0][0], out);
+      win_cluster_merge<NW>(p, b, h, &cpart[0][0], out);
     }
   };
   const bool ok_len = len >= 0 && len <= T * p.max_blocks;
@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(32 * NW, 2) decode_packed_kernel(DecodeParams 
     if (valid) {
       // ---- online softmax (log2 domain)
       tmax = quad_max(tmax);
-      const float m_new = fmaxf(m_run, tmax * qsi);
+      float m_new = fmaxf(m_run, tmax * qsi);
+      if constexpr (WIN != WIN_NONE) m_new = fmaxf(m_new, SEEN);  // every tile of a window call holds a visible token
       const float corr = ex2_ftz(m_run - m_new);
       const float nm = -m_new;
       const float2 nm2 = make_float2(nm, nm), qsi2 = make_float2(qsi, qsi);
@@ -683,10 +684,8 @@ __global__ void __launch_bounds__(128) combine_kernel(DecodeParams p, int rotate
       const float4 a = *reinterpret_cast<const float4*>(pp + PACC + 4 * lane);
       x[0] += f * a.x; x[1] += f * a.y; x[2] += f * a.z; x[3] += f * a.w;
     }
-    const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
-    o = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    if constexpr (WIN)
-      if (M == -INFINITY) o = unreached_row(p.q, wid, p.exp16, lane);
+    const float inv = (WIN || Lsum > 0.f) ? 1.f / Lsum : 0.f;
+    if (!WIN || M != -INFINITY) o = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
   }
   O* dst = out + ((int64_t)b * p.num_q_heads + hq) * D + 4 * lane;
   if (kcheck(dst, 4 * sizeof(O), out, (size_t)batch * p.num_q_heads * D * sizeof(O), p.err)) store4(dst, o);

@@ -259,8 +259,6 @@ kvarn_status kvarn_multiquery_attention(const kvarn_config* cfg, const void* q, 
 // workspace, follow from the arguments alone: 152 SMs.
 static constexpr int kSMs = 152;
 
-static uint32_t exp16(const kvarn_config* cfg) { return cfg->dtype == KVARN_DTYPE_BF16 ? 0x7F80u : 0x7C00u; }
-
 // A window's single query whose sequences visit at most n_vis closed tiles.
 // A small call runs as one cluster per (sequence, KV head): up to seven CTAs
 // of 4 tiles (one per warp) or 8 and one for the open tile, if they are all
@@ -372,14 +370,13 @@ kvarn_status kvarn_window_attention(const kvarn_config* cfg, const void* q, int3
     DecodeParams p{q, block_table, seq_lens, pool, tail_pool, static_cast<float*>(workspace), dev_err,
                    static_cast<int64_t>(kvarn_block_bytes(cfg)), softmax_scale, max_blocks, cfg->num_kv_heads,
                    cfg->num_q_heads, G, cfg->num_blocks, w.chunk, w.n_chunks, cfg->k_bits, cfg->v_bits, 0, 0,
-                   static_cast<int64_t>(workspace_bytes), w.window, w.n_sinks, batch, w.cluster, exp16(cfg)};
+                   static_cast<int64_t>(workspace_bytes), w.window, w.n_sinks, batch, w.cluster};
     return cuda_status(launch_window_decode(p, cfg->dtype, batch, out, out16, static_cast<cudaStream_t>(stream)));
   }
   MQParams p{q, block_table, seq_lens, pool, tail_pool, static_cast<float*>(workspace), dev_err,
              static_cast<int64_t>(kvarn_block_bytes(cfg)), softmax_scale, max_blocks, cfg->num_kv_heads,
              cfg->num_q_heads, G, cfg->num_blocks, n_queries, w.n_rb, w.chunk, w.n_chunks, cfg->k_bits, cfg->v_bits,
              static_cast<int64_t>(workspace_bytes), w.window, w.n_sinks};
-  p.exp16 = exp16(cfg);
   return cuda_status(launch_window_multiquery(p, cfg->dtype, batch, out, out16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -431,7 +428,7 @@ kvarn_status kvarn_tree_attention(const kvarn_config* cfg, const void* q, const 
              static_cast<float*>(workspace), dev_err, static_cast<int64_t>(kvarn_block_bytes(cfg)), softmax_scale,
              max_blocks, cfg->num_kv_heads, cfg->num_q_heads, cfg->num_q_heads / cfg->num_kv_heads, cfg->num_blocks,
              n_nodes, t.n_rb, t.chunk, t.n_chunks, cfg->k_bits, cfg->v_bits, static_cast<int64_t>(workspace_bytes),
-             0, 0, k_draft, v_draft, tree_mask, node_counts, exp16(cfg)};
+             0, 0, k_draft, v_draft, tree_mask, node_counts};
   return cuda_status(launch_tree(p, cfg->dtype, batch, out, out_dtype == KVARN_OUT_16,
                                  static_cast<cudaStream_t>(stream)));
 }

@@ -78,7 +78,6 @@ struct DecodeParams {
   int32_t n_sinks;
   int32_t batch;
   int32_t cluster;  // nonzero: one cluster per (sequence, KV head) merges its own partials
-  uint32_t exp16;   // exponent bits of the 16-bit type
 };
 // Multi-query causal attention: n_queries query tokens per sequence at the
 // last n_queries positions, grouped with their GQA heads into row blocks of
@@ -112,7 +111,6 @@ struct MQParams {
   const void* v_draft;
   const uint64_t* tree_mask;    // [batch][n_queries][ceil(n_queries / 64)]
   const int32_t* node_counts;   // [batch], or null: n_queries each
-  uint32_t exp16;  // window and tree calls: exponent bits of the 16-bit type
 };
 
 // Append of the accepted nodes of a drafted tree (or of several new tokens).

@@ -370,10 +370,8 @@ __global__ void __launch_bounds__(128) mq_combine_kernel(MQParams p, int batch, 
       const float4 a = *reinterpret_cast<const float4*>(pp + MQ_PACC + 4 * lane);
       x[0] += f * a.x; x[1] += f * a.y; x[2] += f * a.z; x[3] += f * a.w;
     }
-    const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
-    o = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    if constexpr (MODE != MQ_CAUSAL)
-      if (M == -INFINITY) o = unreached_row(p.q, wid, p.exp16, lane);
+    const float inv = (MODE != MQ_CAUSAL || Lsum > 0.f) ? 1.f / Lsum : 0.f;
+    if (MODE == MQ_CAUSAL || M != -INFINITY) o = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
   }
   O* dst = out + (((int64_t)b * p.n_queries + qi) * p.num_q_heads + hq) * D + 4 * lane;
   if (kcheck(dst, 4 * sizeof(O), out, (size_t)batch * p.n_queries * p.num_q_heads * D * sizeof(O), p.err))

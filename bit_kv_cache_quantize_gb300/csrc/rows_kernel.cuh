@@ -320,15 +320,16 @@ __global__ void __launch_bounds__(RAW_THREADS, 2) raw_rows_kernel(MQParams p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             sc[nb][e] *= sl2;
-            tmax[e >> 1] = fmaxf(tmax[e >> 1], sc[nb][e]);
+            tmax[e >> 1] = fmaxf(tmax[e >> 1], fmaxf(sc[nb][e], SEEN));
           }
       } else {
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[nb][e] = sees(e >> 1, tb + 8 * nb + 2 * j + (e & 1)) ? sc[nb][e] * sl2 : -INFINITY;
-            tmax[e >> 1] = fmaxf(tmax[e >> 1], sc[nb][e]);
+            const bool in = sees(e >> 1, tb + 8 * nb + 2 * j + (e & 1));
+            sc[nb][e] = in ? sc[nb][e] * sl2 : -INFINITY;
+            tmax[e >> 1] = fmaxf(tmax[e >> 1], in ? fmaxf(sc[nb][e], SEEN) : -INFINITY);
           }
       }
       float corr[2], nm[2], psum[2] = {0.f, 0.f};
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(MQParams p, O* __re
         for (int i = 0; i < 2; ++i)
           if (row_of(i) < rows) {
             all = all && nvis[i] >= T && (MODE != MQ_WINDOW || hs >= min(T, he[i]));
-            dead = dead || m_own[i] == -INFINITY;
+            dead = dead || m_own[i] <= SEEN;
           }
         const bool full = __all_sync(0xffffffffu, all);
         // two scores (log2) less the reference of row i, tokens t, t + 1; hidden ones -inf
@@ -932,7 +933,7 @@ __global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(MQParams p, O* __re
           }
         };
         // The reference this tile starts with: the last one seen.  A warp with
-        // a row that has seen no token yet looks for the tile's maximum first.
+        // a row that has no score yet looks for the tile's maximum first.
         float m_use[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) m_use[i] = m_own[i];
@@ -941,11 +942,14 @@ __global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(MQParams p, O* __re
           top_from(0, top);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (m_own[i] == -INFINITY) m_use[i] = top[i];
+            if (m_own[i] <= SEEN) {
+              const bool sees = nvis[i] > 0 && (hs > 0 || he[i] < nvis[i]);  // some token of this tile
+              m_use[i] = fmaxf(fmaxf(m_own[i], top[i]), sees ? SEEN : -INFINITY);
+            }
         }
         // P~ = p aV, l += sum p, beta += sum p bV in one pass; p may exceed 1.
         // (l counts from the reference too: m_use differs from m_own only
-        // where l is still 0.)
+        // where l is still 0, or NaN.)
         float2 bt[2];
         float emax[2];  // largest exponents of the tile
         auto ref2 = [&](int i) {
@@ -1049,7 +1053,7 @@ __global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(MQParams p, O* __re
             const float em = quad_max(emax[i]);
             const float m_new = em > RQ_RAISE ? m_use[i] + ceilf(em) : m_use[i];
             f[i] = m_new == m_use[i] ? 1.f : pow2_neg(m_new - m_use[i]);
-            corr[i] = m_new == m_own[i] || m_own[i] == -INFINITY ? 1.f : pow2_neg(m_new - m_own[i]);
+            corr[i] = m_new == m_own[i] || m_own[i] <= SEEN ? 1.f : pow2_neg(m_new - m_own[i]);
             any_f = any_f || f[i] != 1.f;
             any_c = any_c || corr[i] != 1.f;
             const float2 f2 = make_float2(f[i], f[i]);
@@ -1147,35 +1151,33 @@ __global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(MQParams p, O* __re
         raw_a[u] = *reinterpret_cast<const float4*>(raw + MQ_PACC + 4 * lane);
       }
     }
-    float x[RU][4], fr[RU], L[RU];
-    bool none[RU];
+    float x[RU][4], fr[RU], inv[RU];
 #pragma unroll
     for (int u = 0; u < RU; ++u) {  // rows behind `rows` hold nothing that counts
       const int r = min(r0 + u * RQ_WARPS, MQ_ROWS - 1);
       const bool live = ok_len && r < rows;
       const float mp = live && n_tiles > 0 ? sm.row_m[r] : -INFINITY, mr = live ? raw_ml[u].x : -INFINITY;
       const float M = fmaxf(mp, mr), m0 = M == -INFINITY ? 0.f : M;
-      none[u] = live && M == -INFINITY;
       const float e = exp2f(mp - m0);
       fr[u] = exp2f(mr - m0);
-      L[u] = fr[u] * raw_ml[u].y;
+      float L = fr[u] * raw_ml[u].y;
       x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
       if (mp != -INFINITY) {
         const float4 a = *reinterpret_cast<const float4*>(rowf + r * RQ_ROWF + 4 * lane);
         const float f = e * INV_SQRT_D;
         x[u][0] = f * a.x; x[u][1] = f * a.y; x[u][2] = f * a.z; x[u][3] = f * a.w;
-        L[u] += e * sm.row_l[r];
+        L += e * sm.row_l[r];
       }
+      inv[u] = M == -INFINITY ? 0.f : 1.f / L;  // a row that sees nothing is zeros
     }
 #pragma unroll
     for (int u = 0; u < RU; ++u) fwht128(x[u], lane);
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
-      const float inv = L[u] > 0.f || L[u] != L[u] ? 1.f / L[u] : 0.f, f = fr[u];
+      const float f = fr[u], iv = inv[u];
       const float4 a = raw_a[u];
-      o[u] = make_float4((x[u][0] + f * a.x) * inv, (x[u][1] + f * a.y) * inv, (x[u][2] + f * a.z) * inv,
-                         (x[u][3] + f * a.w) * inv);
-      if (none[u]) o[u] = unreached_row(p.q, row[u], p.exp16, lane);
+      o[u] = make_float4((x[u][0] + f * a.x) * iv, (x[u][1] + f * a.y) * iv, (x[u][2] + f * a.z) * iv,
+                         (x[u][3] + f * a.w) * iv);
       if (r0 + u * RQ_WARPS >= res_rows) break;
       O* dst = out + row[u] * D + 4 * lane;
       if (kcheck(dst, 4 * sizeof(O), out, (size_t)gridDim.z * p.n_queries * p.num_q_heads * D * sizeof(O), p.err))

@@ -79,8 +79,9 @@ __device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, con
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      sc[nb][e] = seen(tb + 2 * j + e) ? c[e] * sl2 : -INFINITY;
-      m = fmaxf(m, sc[nb][e]);
+      const bool in = seen(tb + 2 * j + e);
+      sc[nb][e] = in ? c[e] * sl2 : -INFINITY;
+      m = fmaxf(m, in ? fmaxf(sc[nb][e], SEEN) : -INFINITY);
     }
   }
   m = quad_max(m);
@@ -183,7 +184,7 @@ __device__ __forceinline__ void cluster_sync_all() {
 // shared memory and writes the result: no workspace, no second launch (3 us of
 // a 12 us call at 8 x 4096 tokens).
 template <int NW, typename O>
-__device__ void win_cluster_merge(const DecodeParams& p, int b, int h, int len, const float* part, O* out) {
+__device__ void win_cluster_merge(const DecodeParams& p, int b, int h, const float* part, O* out) {
   const int n = p.n_chunks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cluster_sync_all();
   const int g = blockIdx.x * NW + warp;  // the cluster spans the grid's x: blockIdx.x is the rank
@@ -210,8 +211,6 @@ __device__ void win_cluster_merge(const DecodeParams& p, int b, int h, int len, 
       const float inv = 1.f / L;
       o = make_float4((x[0] * INV_SQRT_D + y[0]) * inv, (x[1] * INV_SQRT_D + y[1]) * inv,
                       (x[2] * INV_SQRT_D + y[2]) * inv, (x[3] * INV_SQRT_D + y[3]) * inv);
-    } else if (len > 0 && len <= T * p.max_blocks) {
-      o = unreached_row(p.q, (int64_t)b * p.num_q_heads + h * p.G + g, p.exp16, lane);
     }
     O* dst = out + ((int64_t)b * p.num_q_heads + h * p.G + g) * D + 4 * lane;
     if (kcheck(dst, 4 * sizeof(O), out, (size_t)p.batch * p.num_q_heads * D * sizeof(O), p.err)) store4(dst, o);

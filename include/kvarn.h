@@ -271,7 +271,10 @@ size_t kvarn_window_workspace_bytes(const kvarn_config* cfg, int32_t batch, int3
  *  out         device [batch][n_queries][num_q_heads][128], of out_dtype
  *              (kvarn_out_dtype).
  *  workspace   device, >= kvarn_window_workspace_bytes(...) of this shape.
- * Tokens that a row does not see reach nothing of it, whatever they hold.
+ * Tokens that a row does not see reach nothing of it, whatever they hold; a row
+ * whose every score is NaN or -inf is NaN.  (A closed tile is what its records
+ * hold: one quantised from infinities or NaNs may spoil every row of a call
+ * that visits it.)
  * KVARN_ERR_UNSUPPORTED if batch * n_queries * num_q_heads exceeds 2^31 - 1.
  */
 kvarn_status kvarn_window_attention(const kvarn_config* cfg, const void* q, int32_t n_queries,
@@ -309,6 +312,8 @@ size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_
  *                    node that sees nothing (an empty cache and mask) gets
  *                    zeros.
  *  workspace         device, >= kvarn_tree_workspace_bytes(...) of this shape.
+ * Nodes that a node does not see reach nothing of it; one that sees something
+ * and has no score but NaN and -inf gets NaN.
  * A length out of range stores KVARN_DEV_ERR_TOKEN_RANGE and the rows of s
  * are zero (a count out of range: untouched).  Other arguments as
  * kvarn_decode_attention.
