@@ -24,7 +24,10 @@ namespace kvarn {
 // into B fragments (the lane's 64 contiguous bytes of its token; the
 // contraction order is free), the values through shared memory for the
 // transposed load.  Hidden tokens are not loaded, so what they hold (an
-// infinity, a NaN) reaches nothing.
+// infinity, a NaN) reaches nothing.  A visible infinity would meet weights in
+// two parts, one of them 0 or negative, and become NaN: where a warp's sums are
+// not finite it takes such values out, repeats the product and adds them by
+// their whole weights (the test of the sums costs 64 operations a thread).
 template <typename E, int NW>
 __device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, const WinTiles& wt, unsigned char* smem,
                                float* part, int64_t part_stride) {
@@ -50,9 +53,9 @@ __device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, con
       else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
     }
   // k-block kb of QK takes channels 32 j + 4 kb .. + 3 from lane j
+  const E* qb = static_cast<const E*>(p.q) + ((int64_t)b * p.num_q_heads + (int64_t)h * G + g) * D + 32 * j;
   uint32_t qa[16];
   {
-    const E* qb = static_cast<const E*>(p.q) + ((int64_t)b * p.num_q_heads + (int64_t)h * G + g) * D + 32 * j;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint4 v = g < G ? reinterpret_cast<const uint4*>(qb)[i] : make_uint4(0u, 0u, 0u, 0u);
@@ -86,32 +89,75 @@ __device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, con
   }
   m = quad_max(m);
   const float nm = m == -INFINITY ? 0.f : m;  // a warp that sees nothing keeps zero weights
-  float l = 0.f, acc[16][4];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  float l, acc[16][4];
+  uint32_t odd = 0;  // tokens of this warp with values taken out
   cp_async_wait_all();
   __syncwarp();
+#pragma unroll 1
+  for (bool again = false;; again = true) {
+    l = 0.f;
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    uint32_t pa[4];
+    for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      const float x = ex2_ftz(sc[2 * i + nb][0] - nm), y = ex2_ftz(sc[2 * i + nb][1] - nm);
-      l += x + y;
-      uint16_t xh, xl, yh, yl;
-      split_hl<E>(x, xh, xl);
-      split_hl<E>(y, yh, yl);
-      pa[2 * nb] = pack2(xh, yh);
-      pa[2 * nb + 1] = pack2(xl, yl);
+    for (int i = 0; i < NB; ++i) {
+      uint32_t pa[4];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        const float x = ex2_ftz(sc[2 * i + nb][0] - nm), y = ex2_ftz(sc[2 * i + nb][1] - nm);
+        l += x + y;
+        uint16_t xh, xl, yh, yl;
+        split_hl<E>(x, xh, xl);
+        split_hl<E>(y, yh, yl);
+        pa[2 * nb] = pack2(xh, yh);
+        pa[2 * nb + 1] = pack2(xl, yl);
+      }
+      const int r = lane & 15;
+#pragma unroll
+      for (int np = 0; np < 8; ++np) {
+        uint32_t v[4];
+        ldmatrix_x4_trans(v, vs + (16 * i + r) * 256 + (((2 * np + (lane >> 4)) ^ (r & 7)) << 4));
+        mma16816<E>(acc[2 * np], pa, v[0], v[1]);
+        mma16816<E>(acc[2 * np + 1], pa, v[2], v[3]);
+      }
     }
-    const int r = lane & 15;
+    float zero = 0.f;
 #pragma unroll
-    for (int np = 0; np < 8; ++np) {
-      uint32_t v[4];
-      ldmatrix_x4_trans(v, vs + (16 * i + r) * 256 + (((2 * np + (lane >> 4)) ^ (r & 7)) << 4));
-      mma16816<E>(acc[2 * np], pa, v[0], v[1]);
-      mma16816<E>(acc[2 * np + 1], pa, v[2], v[3]);
+    for (int i = 0; i < 16; ++i)
+      zero += (acc[i][0] + acc[i][2]) * 0.f + (acc[i][1] + acc[i][3]) * 0.f;
+    if (again || !__any_sync(0xffffffffu, zero != 0.f)) break;
+    __syncwarp();  // every lane has read the rows
+#pragma unroll 1
+    for (int k = 0; k < NB * 8; ++k) {
+      const int r = 2 * k + (lane >> 4);
+      uint4* x = reinterpret_cast<uint4*>(vs + r * 256 + (((lane & 15) ^ (r & 7)) << 4));
+      uint4 y = *x;
+      bool bad = false;
+      y.x = finite_pair<E>(y.x, bad); y.y = finite_pair<E>(y.y, bad);
+      y.z = finite_pair<E>(y.z, bad); y.w = finite_pair<E>(y.w, bad);
+      if (bad) {
+        *x = y;
+        odd |= 1u << r;
+      }
     }
+    odd = __reduce_or_sync(0xffffffffu, odd);
+    if (!odd) break;  // the weights or the sums themselves are not finite
+    __syncwarp();
+  }
+#pragma unroll 1
+  for (; odd; odd &= odd - 1) {
+    const int k = __ffs(odd) - 1, t = 16 * (warp + NW * (k >> 4)) + (k & 15);
+    float s = 0.f;
+    if (g < G)
+#pragma unroll 1
+      for (int c = 0; c < 32; ++c) s = fmaf(to_f(qb[c]), to_f(kt[t * D + 32 * j + c]), s);
+    const float w = ex2_ftz(quad_sum(s) * (p.scale * LOG2E) - nm);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = to_f(vt[t * D + 8 * i + 2 * j + e]);
+        if (!isfinite(x)) acc[i][e] += w * x;
+      }
   }
   l = quad_sum(l);
   __syncthreads();  // the value rows become the merge area

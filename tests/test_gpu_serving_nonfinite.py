@@ -187,3 +187,24 @@ def test_a_query_that_is_not_finite_gives_nan_in_closed_tiles_alone(kind, n, dty
     bad = torch.zeros(2, n, 4, dtype=torch.bool)
     bad[0, 0, 1] = bad[1, n - 1, 2] = True
     assert (torch.isnan(out).all(-1).cpu() == bad).all() and (torch.isfinite(out).all(-1).cpu() == ~bad).all()
+
+
+@pytest.mark.parametrize("n,lens", [(1, [300, 129]), (1, [300, 129] * 45), (1, [127, 60]), (4, [300, 133]),
+                                    (40, [300, 127])])
+@pytest.mark.parametrize("dtype,out16", [("f16", False), ("bf16", True)])
+def test_values_that_are_not_finite_reach_their_channel_of_the_rows_that_see_them(n, lens, dtype, out16):
+    """Infinities stay infinities, both signs in one channel and NaNs give
+    NaN, and the other channels keep their values."""
+    w = load(lens, dtype, h=1 if len(lens) == 2 else 4, g=5 if n < 40 else 3)
+    c = filled(w)
+    for b, m in enumerate(lens):
+        first = m - m % T
+        for pos, channel, x in ((m - 1, 3, INF), (m - 1, 100, -INF), (m - 20, 0, NAN), (m - 33, 127, -INF),
+                                (m - 40, 50, INF), (m - 41, 50, -INF)):
+            if pos >= first:
+                c.tail[b, :, 1, pos % T, channel] = x
+    q = I.multi_queries(w, n, device="cuda").reshape(w.batch, n, w.num_q_heads, D)
+    out = output(w, n, out16)
+    for window in (1, 30, 200):
+        c.window(q, n, out, window, 0)
+        check(c, q, out, lambda b: visible(lens[b], n, window, 0))
