@@ -241,14 +241,14 @@ __device__ void win_cluster_merge(const DecodeParams& p, int b, int h, const flo
     for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (M != -INFINITY) {
-      const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+      const float f = m == -INFINITY ? -1.f : exp2f(m - M);  // -1: nothing seen, what the partial holds is not defined
       float L = m == -INFINITY ? 0.f : f * cluster_ld(cluster_addr(row + 1, lane));
 #pragma unroll
       for (int s = 16; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
       float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
       for (int i = 0; i <= n; ++i) {
         const float fi = __shfl_sync(0xffffffffu, f, i);
-        if (fi == 0.f) continue;  // nothing seen: what the partial holds is not defined
+        if (fi < 0.f) continue;  // (a weight of 0 counts: 0 times an infinity is NaN)
         const float4 a = cluster_ld4(cluster_addr(row + PACC + 4 * lane, i));
         float* z = i == n ? y : x;
         z[0] += fi * a.x; z[1] += fi * a.y; z[2] += fi * a.z; z[3] += fi * a.w;

@@ -208,3 +208,39 @@ def test_values_that_are_not_finite_reach_their_channel_of_the_rows_that_see_the
     for window in (1, 30, 200):
         c.window(q, n, out, window, 0)
         check(c, q, out, lambda b: visible(lens[b], n, window, 0))
+
+
+@pytest.mark.parametrize("kind,n,batch", [("window", 1, 2), ("window", 1, 90), ("window", 4, 2), ("tree", 4, 2)])
+@pytest.mark.parametrize("dtype,out16", [("f16", False), ("bf16", True)])
+@pytest.mark.parametrize("near", [False, True])
+def test_values_of_weight_zero_are_not_lost(kind, n, batch, dtype, out16, near):
+    """A closed tile's scores (near: also those of two open-tile tokens) lie
+    hundreds of powers of two above the open tile's, so those weights are 0 in
+    fp32; what is not finite there still reaches the rows that see it (as 0
+    times it: NaN)."""
+    w = load([128 + 40] * batch, dtype, h=1 if batch == 2 else 4, g=2)
+    c = PagedCache(w, device())
+    u = torch.from_numpy(np.where(np.random.default_rng(1).random(D) < 0.5, 1.0, -1.0)).cuda()
+    for b in range(batch):
+        k = normal16(b, (168, w.num_kv_heads, D), dtype)
+        k[:T] = (8 * u + 0.05 * k[:T]).to(k.dtype)
+        k[T:] *= 0.01
+        if near:
+            k[T + 6] = k[T + 36] = (8 * u).to(k.dtype)
+        c.quantize_sequence(b, k, normal16(b + 99, (168, w.num_kv_heads, D), dtype))
+    c.tail[0, :, 1, 5, 9] = INF
+    c.tail[1, :, 1, 35, 33] = NAN
+    q = (8 * u).to(I.torch_dtype(dtype)).expand(batch, n, w.num_q_heads, D).contiguous()
+    kd, vd = (normal16(s, (batch, n, w.num_kv_heads, D), dtype) for s in (1, 2))
+    vd[1, 2 % n, :, 70] = -INF
+    out = output(w, n, out16)
+    if kind == "tree":
+        c.tree(q, kd, vd, torch.full((batch, n, 1), -1, dtype=torch.int64, device="cuda"), out)
+    else:
+        c.window(q, n, out, 400, 0)
+    torch.cuda.synchronize()
+    assert c.check_error() == 0
+    bad = torch.zeros(batch, D, dtype=torch.bool)
+    bad[0, 9] = bad[1, 33] = True
+    bad[1, 70] = kind == "tree"
+    assert ((~torch.isfinite(out)).cpu() == bad[:, None, None].expand(out.shape)).all()
