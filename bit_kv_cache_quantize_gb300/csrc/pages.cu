@@ -471,15 +471,16 @@ cudaError_t launch_fork_sequences(const ForkParams& p, cudaStream_t s) {
 }
 
 size_t pages_ws_bytes(int64_t num_blocks) {
-  const int64_t chunks = (num_blocks + CP_CHUNK - 1) / CP_CHUNK;
+  // ranks, and the counts of the chunks: an empty pool has one too
+  const int64_t chunks = std::max<int64_t>((num_blocks + CP_CHUNK - 1) / CP_CHUNK, 1);
   return (size_t)((num_blocks + chunks + 3) / 4 * 16);
 }
 
 cudaError_t launch_compact(const PageParams& p, cudaStream_t s) {
-  const int chunks = (int)(((int64_t)p.num_blocks + CP_CHUNK - 1) / CP_CHUNK);
-  cudaError_t e = launch_after(compact_count_kernel, dim3(std::max(chunks, 1)), dim3(CP_THREADS), s, p);
+  const int chunks = (int)std::max<int64_t>(((int64_t)p.num_blocks + CP_CHUNK - 1) / CP_CHUNK, 1);
+  cudaError_t e = launch_after(compact_count_kernel, dim3(chunks), dim3(CP_THREADS), s, p);
   if (e != cudaSuccess) return e;
-  e = launch_after(compact_plan_kernel, dim3(std::max(chunks, 1)), dim3(CP_THREADS), s, p, chunks);
+  e = launch_after(compact_plan_kernel, dim3(chunks), dim3(CP_THREADS), s, p, chunks);
   if (e != cudaSuccess) return e;
   const int64_t work = std::max<int64_t>((int64_t)p.batch * p.max_blocks, p.num_blocks);
   const unsigned grid = (unsigned)std::min<int64_t>(std::max<int64_t>((work + CP_THREADS - 1) / CP_THREADS, 1), 152 * 8);

@@ -180,3 +180,16 @@ def test_checked_build_reports_nothing_and_gives_the_same_bits(dtype, kb, vb):
         checked = run_all(dtype, kb, vb, dev)
     for key, x in plain.items():
         assert torch.equal(x.reshape(-1).view(torch.uint8), checked[key].reshape(-1).view(torch.uint8)), key
+
+
+def test_compaction_of_an_empty_pool_stays_in_its_workspace():
+    dev = device()
+    cfg = K.make_config(2, 4, 0, "f16")
+    h = Held(dev)
+    err = h.writes(torch.zeros(1, dtype=torch.int32, device=dev), "dev_err")
+    table = h.reads(torch.full((3, 5), -1, dtype=torch.int32, device=dev), "table")
+    counts = h.writes(torch.full((2,), 7, dtype=torch.int32, device=dev), "counts")
+    need = K.kvarn_pages_workspace_bytes(cfg, 3)
+    K.kvarn_compact_blocks(cfg, table, 5, 3, None, None, None, counts, h.space(need), need, err)
+    h.check(err)
+    assert counts.tolist() == [0, 0]

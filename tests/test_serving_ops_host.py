@@ -180,3 +180,13 @@ def test_calls_of_many_shapes_share_workspaces():
     assert c._workspace("window", 100).data_ptr() in seen
     big = c._workspace("tree", 1 << 20)
     assert big.data_ptr() not in seen and c._workspace("tree", 5).data_ptr() == big.data_ptr()
+
+
+def test_pages_of_an_empty_pool_have_a_workspace():
+    """Its one chunk count is stored as any other."""
+    cfg = K.make_config(8, 64, 0, "f16")
+    assert K.kvarn_pages_workspace_bytes(cfg, 4) == 16
+
+    def compact(size):
+        return K.kvarn_compact_blocks(cfg, 16, 40, 4, None, None, None, 16, 16, size, 16, stream=0, check=False)
+    assert compact(0) == INV and compact(15) == INV
