@@ -86,10 +86,11 @@ __global__ void __launch_bounds__(PG_THREADS) alloc_kernel(PageParams p) {
   uint32_t next = free_bits(p, (int64_t)tid * AL_IDS);
   int32_t* open = p.ws;  // [need] the open entries, as offsets into the table
   int need = 0;
-  for (int s0 = 0; s0 < p.batch; s0 += PG_THREADS) {
-    const int s = s0 + tid;
+  // (counters up to 2^31 - 1 in steps of the block: unsigned, the last step passes it)
+  for (uint32_t s0 = 0; s0 < (uint32_t)p.batch; s0 += PG_THREADS) {
+    const uint32_t s = s0 + tid;
     int t0 = 0, t1 = 0;
-    if (s < p.batch && !tile_range(p, s, t0, t1)) {
+    if (s < (uint32_t)p.batch && !tile_range(p, (int)s, t0, t1)) {
       set_error(p.err, KVARN_DEV_ERR_TOKEN_RANGE);
       t0 = t1 = 0;
     }
@@ -98,15 +99,15 @@ __global__ void __launch_bounds__(PG_THREADS) alloc_kernel(PageParams p) {
     first[tid] = before;
     begin[tid] = t0;
     __syncthreads();
-    for (int e0 = 0; e0 < total; e0 += PG_THREADS) {
-      const int e = e0 + tid;
+    for (uint32_t e0 = 0; e0 < (uint32_t)total; e0 += PG_THREADS) {
+      const uint32_t e = e0 + tid;
       int at = -1;
-      if (e < total) {
+      if (e < (uint32_t)total) {
         int lo = 0;  // the last sequence that starts at or before e (an empty range shares its start with the next)
 #pragma unroll
         for (int step = PG_THREADS / 2; step > 0; step >>= 1)
-          if (first[lo + step] <= e) lo += step;
-        const int off = (s0 + lo) * p.max_blocks + begin[lo] + e - first[lo];
+          if (first[lo + step] <= (int)e) lo += step;
+        const int off = (int)(s0 + lo) * p.max_blocks + begin[lo] + (int)e - first[lo];
         if (p.table[off] < 0) at = off;
       }
       int all;

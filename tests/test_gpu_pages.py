@@ -256,3 +256,24 @@ def test_compact_reports_a_low_block_without_count():
     c.compact()
     torch.cuda.synchronize()
     assert c.check_error() == K.KVARN_DEV_ERR_REF_COUNT
+
+
+@pytest.mark.parametrize("batch,columns", [(128, (1 << 24) - 1), (2 ** 31 - 1, 1)])
+def test_alloc_at_the_largest_tables(batch, columns):
+    """Tables of 2^31 - 128 and 2^31 - 1 entries, open ones at both ends."""
+    dev = device()
+    cfg = K.make_config(1, 1, 9, "f16")
+    table = torch.zeros(batch, columns, dtype=torch.int32, device=dev)
+    refs = torch.tensor([7, 0, 1, 0, 0, 1, 0, 0, 1], dtype=torch.int32, device=dev)
+    table[0, 0] = table[-1, -1] = table[batch // 2, columns // 2] = -1
+    begin = torch.zeros(batch, dtype=torch.int32, device=dev)
+    end = torch.full((batch,), columns, dtype=torch.int32, device=dev)
+    need = K.kvarn_pages_workspace_bytes(cfg, batch)
+    ws, err = torch.empty(need, dtype=torch.uint8, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    K.kvarn_alloc_blocks(cfg, table, columns, batch, begin, end, refs, ws, need, err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    assert [int(table[0, 0]), int(table[batch // 2, columns // 2]), int(table[-1, -1])] == [1, 3, 4]
+    assert refs.tolist() == [7, 1, 1, 1, 1, 1, 0, 0, 1]
+    table[0, 0] = table[-1, -1] = table[batch // 2, columns // 2] = 0
+    assert not table.any()
