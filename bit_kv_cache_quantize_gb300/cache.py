@@ -10,6 +10,8 @@ configuration and the generated inputs are those of that head range.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import inputs as I
@@ -100,24 +102,37 @@ class PagedCache:
                                       self.w.batch, self.pool16, self.w.scale, out, self.ws, self.ws_bytes,
                                       self.err, stream)
 
-    def _keep(self, key, make):
-        """A buffer made on first use.  It is never replaced, so a captured
-        graph may go on using it; making one inside a capture is refused (it
-        would live in that graph's private memory)."""
+    @staticmethod
+    def _on(stream):
+        """The context in which torch's work (and the memory it hands out) is
+        ordered with a call on `stream` (None: the current one, a torch stream
+        or a raw handle)."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        return torch.cuda.stream(stream)
+
+    def _keep(self, key, make, stream=None):
+        """A buffer made on first use, on the stream of the call that needs it
+        first.  It is never replaced, so a captured graph may go on using it;
+        making one inside a capture is refused (it would live in that graph's
+        private memory)."""
         if key not in self._kept:
-            if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("run the call once before capturing it: its workspace does not exist yet")
-            self._kept[key] = make()
+            with self._on(stream):
+                if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("run the call once before capturing it: its workspace does not exist yet")
+                self._kept[key] = make()
         return self._kept[key]
 
-    def _workspace(self, op: str, need: int):
+    def _workspace(self, op: str, need: int, stream=None):
         """The smallest workspace of `op` that holds `need` bytes; a new one
         has a power of two of them (64 KiB or more), so calls of every shape leave a few
         buffers behind, not one each."""
         size = 1 << max(need - 1, 0xFFFF).bit_length()
         held = [k[1] for k in self._kept if type(k) is tuple and k[0] == op and k[1] >= size]
         return self._keep((op, min(held, default=size)),
-                          lambda: torch.empty(size, dtype=torch.uint8, device=self.device))
+                          lambda: torch.empty(size, dtype=torch.uint8, device=self.device), stream)
 
     def _out_dtype(self, out) -> int:
         if out.dtype == torch.float32:
@@ -143,7 +158,7 @@ class PagedCache:
         if out.numel() != q.numel():
             raise ValueError(f"out has {out.numel()} elements, q {q.numel()}")
         need = K.kvarn_window_workspace_bytes(self.cfg, self.w.batch, self.max_blocks, n_queries, window, n_sinks)
-        ws = self._workspace("window", need)
+        ws = self._workspace("window", need, stream)
         K.kvarn_window_attention(self.cfg, q, n_queries, self.table, self.max_blocks,
                                  self.lens if lens is None else lens, self.w.batch, window, n_sinks, self.pool,
                                  self.tail, self.w.scale, out, kind, ws, need, self.err, stream)
@@ -162,7 +177,7 @@ class PagedCache:
         if out.numel() != q.numel():
             raise ValueError(f"out has {out.numel()} elements, q {q.numel()}")
         need = K.kvarn_tree_workspace_bytes(self.cfg, self.w.batch, self.max_blocks, n)
-        ws = self._workspace("tree", need)
+        ws = self._workspace("tree", need, stream)
         K.kvarn_tree_attention(self.cfg, q, k_draft, v_draft, mask, n, counts, self.table, self.max_blocks,
                                self.lens if lens is None else lens, self.w.batch, self.pool, self.tail, self.w.scale,
                                out, kind, ws, need, self.err, stream)
@@ -183,32 +198,38 @@ class PagedCache:
     @property
     def refs(self):
         """Reference counts of the blocks, from the table on first use."""
+        return self._refs()
+
+    def _refs(self, stream=None):
         def make():
             ids = self.table[self.table >= 0].long()
             return torch.bincount(ids, minlength=self.num_blocks).to(torch.int32).contiguous()
-        return self._keep("refs", make)
+        return self._keep("refs", make, stream)
 
     def alloc(self, tile_begin, tile_end, stream=None):
         """Give the open entries of tiles [tile_begin[b], tile_end[b]) free blocks."""
         need = K.kvarn_pages_workspace_bytes(self.cfg, self.w.batch)
-        K.kvarn_alloc_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, tile_begin, tile_end, self.refs,
-                             self._workspace("pages", need), need, self.err, stream)
+        K.kvarn_alloc_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, tile_begin, tile_end,
+                             self._refs(stream), self._workspace("pages", need, stream), need, self.err, stream)
 
     def free(self, tile_begin, tile_end, stream=None):
         """Release the blocks of tiles [tile_begin[b], tile_end[b])."""
-        K.kvarn_free_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, tile_begin, tile_end, self.refs,
-                            self.err, stream)
+        K.kvarn_free_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, tile_begin, tile_end,
+                            self._refs(stream), self.err, stream)
 
     def free_behind_window(self, lens, window, n_sinks=0, stream=None):
         """Release the tiles that no query at position lens[b] - 1 or later sees."""
-        begin = torch.full_like(lens, min(-(-n_sinks // T), self.max_blocks))
-        self.free(begin, ((lens - window).clamp_min(0) // T).to(torch.int32), stream)
+        with self._on(stream):  # the ranges are written, and their memory reused, in the order of the call's stream
+            begin = torch.full_like(lens, min(-(-n_sinks // T), self.max_blocks))
+            end = ((lens - window).clamp_min(0) // T).to(torch.int32)
+            self.free(begin, end, stream)
+            del begin, end
 
     def fork(self, parent, group, lens=None, stream=None):
         """Slot b takes the sequence of slot parent[b] (within its group of
         `group` slots; -1 empties it): open tiles, table rows, counts, lens."""
         lens = self.lens if lens is None else lens
-        refs = self.refs
+        refs = self._refs(stream)
         K.kvarn_fork_tails(self.cfg, parent, group, self.w.batch, lens, self.max_blocks, self.tail, self.err, stream)
         K.kvarn_fork_sequences(self.cfg, parent, group, self.w.batch, self.table, self.max_blocks, lens, refs,
                                self.err, stream)
@@ -217,11 +238,12 @@ class PagedCache:
         """Move the live blocks to ids 0 .. L - 1; returns the device counts
         (L, moves)."""
         need = K.kvarn_pages_workspace_bytes(self.cfg, self.w.batch)
-        ws = self._workspace("pages", need)
-        moves = self._keep("moves", lambda: torch.empty(2, self.num_blocks, dtype=torch.int32, device=self.device))
-        counts = self._keep("counts", lambda: torch.zeros(2, dtype=torch.int32, device=self.device))
-        K.kvarn_compact_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, self.refs, moves[0], moves[1],
-                               counts, ws, need, self.err, stream)
+        ws = self._workspace("pages", need, stream)
+        moves = self._keep("moves", lambda: torch.empty(2, self.num_blocks, dtype=torch.int32, device=self.device),
+                           stream)
+        counts = self._keep("counts", lambda: torch.zeros(2, dtype=torch.int32, device=self.device), stream)
+        K.kvarn_compact_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, self._refs(stream), moves[0],
+                               moves[1], counts, ws, need, self.err, stream)
         K.kvarn_copy_blocks(self.cfg, self.pool, self.num_blocks, moves[0], self.pool, moves[1], self.num_blocks,
                             counts[1:], self.err, stream)
         return counts

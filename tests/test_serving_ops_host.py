@@ -190,3 +190,47 @@ def test_pages_of_an_empty_pool_have_a_workspace():
     def compact(size):
         return K.kvarn_compact_blocks(cfg, 16, 40, 4, None, None, None, 16, 16, size, 16, stream=0, check=False)
     assert compact(0) == INV and compact(15) == INV
+
+
+def test_what_a_call_makes_is_made_on_its_stream(monkeypatch):
+    """Ranges, counts and workspaces that a call with stream= makes by torch
+    are ordered with its kernels: made while that stream is the current one."""
+    import contextlib
+    active, made = [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        active.append(s)
+        yield
+        active.pop()
+
+    def noted(name):
+        real = getattr(torch, name)
+
+        def f(*a, **kw):
+            made.append((name, active[-1] if active else None))
+            return real(*a, **kw)
+        return f
+    w = I.Workload("streams", 2, 8, 2, "f16", [300, 200], seed=1, max_tokens=301)
+    c = PagedCache(w, "cpu")
+    q = torch.zeros(2, 3, 8, 128, dtype=torch.float16)
+    kv = torch.zeros(2, 3, 2, 128, dtype=torch.float16)
+    mask, parent = torch.zeros(2, 3, 1, dtype=torch.int64), torch.zeros(2, dtype=torch.int32)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for name in ("full_like", "bincount", "zeros", "empty"):
+        monkeypatch.setattr(torch, name, noted(name))
+    for name in K.EXPORTS:
+        if not name.endswith("_bytes"):
+            monkeypatch.setattr(K, name, lambda *a, **kw: 0)
+    s = object()
+    for call in (lambda: c.free_behind_window(c.lens, 100, 4, stream=s), lambda: c.compact(stream=s),
+                 lambda: c.window(q, 3, q, 100, stream=s), lambda: c.tree(q, kv, kv, mask, q, stream=s)):
+        made.clear()
+        call()
+        assert made and all(at is s for _, at in made), made
+    c._kept.clear()
+    for call in (lambda: c.alloc(parent, parent, stream=s), lambda: c.fork(parent, 2, stream=s)):
+        c._kept.pop("refs", None)
+        made.clear()
+        call()
+        assert made and all(at is s for _, at in made), made
