@@ -125,30 +125,46 @@ def _p(x):
     return x.data_ptr()
 
 
-def _c(x):
-    """_p of a tensor that has to be contiguous and on the GPU (the window,
-    tree and page calls take no strides).  A tenth of a microsecond each: ten
-    tensors a call, and small calls are as long as their host part."""
+_device_calls = None
+
+
+def _here():
+    """The current CUDA device, whose context and stream a launch uses; -2
+    (no tensor lies there) without one."""
+    global _device_calls
+    if _device_calls is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -2
+        torch.cuda.init()
+        _device_calls = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device_calls()
+
+
+def _c(x, here):
+    """_p of a tensor that has to be contiguous and on the current device (the
+    window, tree and page calls take no strides).  A tenth of a microsecond
+    each: ten tensors a call, and small calls are as long as their host part."""
     if x is None or type(x) is int:
         return x
-    if x.is_cuda and x.is_contiguous():
+    if x.get_device() == here and x.is_contiguous():
         return x.data_ptr()
-    return _refuse(x)
+    return _refuse(x, here)
 
 
 _int32 = None  # torch.int32, once torch is in use
 
 
-def _i(x):
+def _i(x, here):
     """_c of an int32 array (table, lengths, counts, ids)."""
     if x is None or type(x) is int:
         return x
-    if x.dtype is _int32 and x.is_cuda and x.is_contiguous():
+    if x.dtype is _int32 and x.get_device() == here and x.is_contiguous():
         return x.data_ptr()
-    return _refuse(x, True)
+    return _refuse(x, here, True)
 
 
-def _refuse(x, int32=False):
+def _refuse(x, here, int32=False):
     global _int32
     if isinstance(x, int):
         return x
@@ -161,6 +177,8 @@ def _refuse(x, int32=False):
         raise ValueError(f"a contiguous tensor is needed, got shape {tuple(x.shape)} with strides {x.stride()}")
     if not x.is_cuda:
         raise ValueError(f"a tensor on the GPU is needed, got one on {x.device}")
+    if x.get_device() != here:
+        raise ValueError(f"a tensor on {x.device}, but the current device is cuda:{here}")
     return x.data_ptr()
 
 
@@ -184,17 +202,6 @@ def _s(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-def _d(x, stream):
-    """The stream of a call whose tensors lie where x does: they have to lie
-    on the current device, whose stream (and context) the launch uses."""
-    s = _s(stream)
-    if x is not None and not isinstance(x, int):
-        dev = _stream_calls[1]() if _stream_calls else None
-        if not x.is_cuda or (dev is not None and x.get_device() != dev):
-            raise ValueError(f"tensors on {x.device}, but the current device is cuda:{dev}")
-    return s
 
 
 def _check(status: int, fn: str, check: bool) -> int:
@@ -323,10 +330,11 @@ def kvarn_window_attention(cfg, q, n_queries, block_table, max_blocks, seq_lens,
                            check=True) -> int:
     """The last n_queries tokens of every sequence over the last `window`
     tokens up to their own and the first n_sinks (see include/kvarn.h)."""
-    st = lib().kvarn_window_attention(ctypes.byref(cfg), _c(q), int(n_queries), _i(block_table), int(max_blocks),
-                                      _i(seq_lens), int(batch), int(window), int(n_sinks), _c(block_pool),
-                                      _c(tail_pool), float(softmax_scale), _c(out), int(out_dtype), _c(workspace),
-                                      int(workspace_bytes), _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_window_attention(ctypes.byref(cfg), _c(q, d), int(n_queries), _i(block_table, d), int(max_blocks),
+                                      _i(seq_lens, d), int(batch), int(window), int(n_sinks), _c(block_pool, d),
+                                      _c(tail_pool, d), float(softmax_scale), _c(out, d), int(out_dtype),
+                                      _c(workspace, d), int(workspace_bytes), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_window_attention", check)
 
 
@@ -339,10 +347,12 @@ def kvarn_tree_attention(cfg, q, k_draft, v_draft, tree_mask, n_nodes, node_coun
                          dev_err, stream=None, check=True) -> int:
     """The nodes of a drafted tree over the cache and the nodes their mask
     rows name (tree_mask: 64-bit words; see include/kvarn.h)."""
-    st = lib().kvarn_tree_attention(ctypes.byref(cfg), _c(q), _c(k_draft), _c(v_draft), _c(tree_mask), int(n_nodes),
-                                    _i(node_counts), _i(block_table), int(max_blocks), _i(seq_lens), int(batch),
-                                    _c(block_pool), _c(tail_pool), float(softmax_scale), _c(out), int(out_dtype),
-                                    _c(workspace), int(workspace_bytes), _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_tree_attention(ctypes.byref(cfg), _c(q, d), _c(k_draft, d), _c(v_draft, d), _c(tree_mask, d),
+                                    int(n_nodes), _i(node_counts, d), _i(block_table, d), int(max_blocks),
+                                    _i(seq_lens, d), int(batch), _c(block_pool, d), _c(tail_pool, d),
+                                    float(softmax_scale), _c(out, d), int(out_dtype), _c(workspace, d),
+                                    int(workspace_bytes), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_tree_attention", check)
 
 
@@ -350,9 +360,10 @@ def kvarn_commit_tokens(cfg, k_draft, v_draft, n_nodes, path, max_path, path_len
                         tail_pool, block_pool, dev_err, stream=None, check=True) -> int:
     """Append nodes path[s][0 .. path_lens[s]) of the draft arrays (path
     None: the first path_lens[s] nodes) at positions pos[s] ...."""
-    st = lib().kvarn_commit_tokens(ctypes.byref(cfg), _c(k_draft), _c(v_draft), int(n_nodes), _i(path), int(max_path),
-                                   _i(path_lens), _i(pos), _i(block_table), int(max_blocks), int(batch),
-                                   _c(tail_pool), _c(block_pool), _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_commit_tokens(ctypes.byref(cfg), _c(k_draft, d), _c(v_draft, d), int(n_nodes), _i(path, d),
+                                   int(max_path), _i(path_lens, d), _i(pos, d), _i(block_table, d), int(max_blocks),
+                                   int(batch), _c(tail_pool, d), _c(block_pool, d), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_commit_tokens", check)
 
 
@@ -363,33 +374,37 @@ def kvarn_pages_workspace_bytes(cfg, batch: int) -> int:
 def kvarn_alloc_blocks(cfg, block_table, max_blocks, batch, tile_begin, tile_end, refs, workspace, workspace_bytes,
                        dev_err, stream=None, check=True) -> int:
     """Lowest free blocks for the open entries of each sequence's tile range."""
-    st = lib().kvarn_alloc_blocks(ctypes.byref(cfg), _i(block_table), int(max_blocks), int(batch), _i(tile_begin),
-                                  _i(tile_end), _i(refs), _c(workspace), int(workspace_bytes), _i(dev_err),
-                                  _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_alloc_blocks(ctypes.byref(cfg), _i(block_table, d), int(max_blocks), int(batch), _i(tile_begin, d),
+                                  _i(tile_end, d), _i(refs, d), _c(workspace, d), int(workspace_bytes), _i(dev_err, d),
+                                  _s(stream))
     return _check(st, "kvarn_alloc_blocks", check)
 
 
 def kvarn_free_blocks(cfg, block_table, max_blocks, batch, tile_begin, tile_end, refs, dev_err, stream=None,
                       check=True) -> int:
     """Release the blocks of each sequence's tile range."""
-    st = lib().kvarn_free_blocks(ctypes.byref(cfg), _i(block_table), int(max_blocks), int(batch), _i(tile_begin),
-                                 _i(tile_end), _i(refs), _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_free_blocks(ctypes.byref(cfg), _i(block_table, d), int(max_blocks), int(batch), _i(tile_begin, d),
+                                 _i(tile_end, d), _i(refs, d), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_free_blocks", check)
 
 
 def kvarn_fork_tails(cfg, parent, group, batch, seq_lens, max_blocks, tail_pool, dev_err, stream=None,
                      check=True) -> int:
     """Open tiles of one layer: slot s takes its parent's (before kvarn_fork_sequences)."""
-    st = lib().kvarn_fork_tails(ctypes.byref(cfg), _i(parent), int(group), int(batch), _i(seq_lens), int(max_blocks),
-                                _c(tail_pool), _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_fork_tails(ctypes.byref(cfg), _i(parent, d), int(group), int(batch), _i(seq_lens, d),
+                                int(max_blocks), _c(tail_pool, d), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_fork_tails", check)
 
 
 def kvarn_fork_sequences(cfg, parent, group, batch, block_table, max_blocks, seq_lens, refs, dev_err, stream=None,
                          check=True) -> int:
     """Table rows, reference counts and lengths: slot s takes its parent's sequence."""
-    st = lib().kvarn_fork_sequences(ctypes.byref(cfg), _i(parent), int(group), int(batch), _i(block_table),
-                                    int(max_blocks), _i(seq_lens), _i(refs), _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_fork_sequences(ctypes.byref(cfg), _i(parent, d), int(group), int(batch), _i(block_table, d),
+                                    int(max_blocks), _i(seq_lens, d), _i(refs, d), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_fork_sequences", check)
 
 
@@ -397,15 +412,17 @@ def kvarn_compact_blocks(cfg, block_table, max_blocks, batch, refs, move_src, mo
                          workspace_bytes, dev_err, stream=None, check=True) -> int:
     """Plan a compaction and rewrite table and counts; kvarn_copy_blocks then
     moves each layer's records (move_src -> move_dst, counts[1] of them)."""
-    st = lib().kvarn_compact_blocks(ctypes.byref(cfg), _i(block_table), int(max_blocks), int(batch), _i(refs),
-                                    _i(move_src), _i(move_dst), _i(counts), _c(workspace), int(workspace_bytes),
-                                    _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_compact_blocks(ctypes.byref(cfg), _i(block_table, d), int(max_blocks), int(batch), _i(refs, d),
+                                    _i(move_src, d), _i(move_dst, d), _i(counts, d), _c(workspace, d),
+                                    int(workspace_bytes), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_compact_blocks", check)
 
 
 def kvarn_copy_blocks(cfg, src_pool, src_blocks, src_ids, dst_pool, dst_ids, n, n_dev, dev_err, stream=None,
                       check=True) -> int:
     """Records of blocks src_ids of src_pool to blocks dst_ids of dst_pool."""
-    st = lib().kvarn_copy_blocks(ctypes.byref(cfg), _c(src_pool), int(src_blocks), _i(src_ids), _c(dst_pool),
-                                 _i(dst_ids), int(n), _i(n_dev), _i(dev_err), _d(dev_err, stream))
+    d = _here()
+    st = lib().kvarn_copy_blocks(ctypes.byref(cfg), _c(src_pool, d), int(src_blocks), _i(src_ids, d), _c(dst_pool, d),
+                                 _i(dst_ids, d), int(n), _i(n_dev, d), _i(dev_err, d), _s(stream))
     return _check(st, "kvarn_copy_blocks", check)

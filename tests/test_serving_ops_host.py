@@ -234,3 +234,46 @@ def test_what_a_call_makes_is_made_on_its_stream(monkeypatch):
         made.clear()
         call()
         assert made and all(at is s for _, at in made), made
+
+
+class Elsewhere:
+    """Stands for an int32 tensor on the second GPU."""
+    dtype, device, is_cuda, shape = torch.int32, torch.device("cuda:1"), True, (4,)
+
+    def get_device(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return (1,)
+
+    def data_ptr(self):
+        return 16
+
+
+CALLS = {  # arguments of each call; 16 stands for a device pointer
+    "kvarn_window_attention": (16, 1, 16, 40, 16, 0, 200, 4, 16, 16, 0.1, 16, 0, 16, 1 << 40, 16),
+    "kvarn_tree_attention": (16, 16, 16, 16, 8, 16, 16, 40, 16, 0, 16, 16, 0.1, 16, 1, 16, 1 << 40, 16),
+    "kvarn_commit_tokens": (16, 16, 8, 16, 5, 16, 16, 16, 40, 0, 16, 16, 16),
+    "kvarn_alloc_blocks": (16, 40, 0, 16, 16, 16, 16, 1 << 40, 16),
+    "kvarn_free_blocks": (16, 40, 0, 16, 16, 16, 16),
+    "kvarn_fork_tails": (16, 2, 0, 16, 40, 16, 16),
+    "kvarn_fork_sequences": (16, 2, 0, 16, 40, 16, 16, 16),
+    "kvarn_compact_blocks": (16, 40, 0, 16, 16, 16, 16, 16, 1 << 40, 16),
+    "kvarn_copy_blocks": (16, 9, 16, 16, 16, 0, 16, 16),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_every_tensor_has_to_lie_on_the_current_device(name, monkeypatch):
+    monkeypatch.setattr(K, "_here", lambda: 0, raising=False)
+    call, args = getattr(K, name), CALLS[name]
+    assert call(BAD, *args, stream=0, check=False) == UNS  # (a configuration that the library refuses: no launch)
+    for i, x in enumerate(args):
+        if x == 16:
+            with pytest.raises(ValueError, match="cuda:1, but the current device is cuda:0"):
+                call(BAD, *args[:i], Elsewhere(), *args[i + 1:], stream=0, check=False)
+    monkeypatch.setattr(K, "_here", lambda: 1, raising=False)
+    assert call(BAD, *(Elsewhere() if x == 16 else x for x in args), stream=0, check=False) == UNS
