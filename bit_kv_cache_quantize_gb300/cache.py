@@ -148,6 +148,13 @@ class PagedCache:
             raise ValueError(f"{name} is {want} {I.torch_dtype(self.w.dtype)}, got {tuple(q.shape)} {q.dtype}")
         return q
 
+    def _each(self, x, name, width=1):
+        """x as `width` entries per sequence: a shorter array would be read
+        past its end on the device."""
+        if x.numel() != self.w.batch * width:
+            raise ValueError(f"{name} has {width} per sequence of {self.w.batch}, got {tuple(x.shape)}")
+        return x
+
     def window(self, q, n_queries, out, window, n_sinks=0, lens=None, stream=None):
         """q [B][n_queries][Hq][D]: the last n_queries tokens of each sequence
         attend to the last `window` tokens up to their own and the first
@@ -157,10 +164,10 @@ class PagedCache:
         kind = self._out_dtype(out)
         if out.numel() != q.numel():
             raise ValueError(f"out has {out.numel()} elements, q {q.numel()}")
+        lens = self._each(self.lens if lens is None else lens, "lens")
         need = K.kvarn_window_workspace_bytes(self.cfg, self.w.batch, self.max_blocks, n_queries, window, n_sinks)
         ws = self._workspace("window", need, stream)
-        K.kvarn_window_attention(self.cfg, q, n_queries, self.table, self.max_blocks,
-                                 self.lens if lens is None else lens, self.w.batch, window, n_sinks, self.pool,
+        K.kvarn_window_attention(self.cfg, q, n_queries, self.table, self.max_blocks, lens, self.w.batch, window, n_sinks, self.pool,
                                  self.tail, self.w.scale, out, kind, ws, need, self.err, stream)
 
     def tree(self, q, k_draft, v_draft, mask, out, counts=None, lens=None, stream=None):
@@ -176,10 +183,13 @@ class PagedCache:
         kind = self._out_dtype(out)
         if out.numel() != q.numel():
             raise ValueError(f"out has {out.numel()} elements, q {q.numel()}")
+        lens = self._each(self.lens if lens is None else lens, "lens")
+        if counts is not None:
+            self._each(counts, "counts")
         need = K.kvarn_tree_workspace_bytes(self.cfg, self.w.batch, self.max_blocks, n)
         ws = self._workspace("tree", need, stream)
         K.kvarn_tree_attention(self.cfg, q, k_draft, v_draft, mask, n, counts, self.table, self.max_blocks,
-                               self.lens if lens is None else lens, self.w.batch, self.pool, self.tail, self.w.scale,
+                               lens, self.w.batch, self.pool, self.tail, self.w.scale,
                                out, kind, ws, need, self.err, stream)
 
     # ------------------------------------------------------------ drafts
@@ -190,6 +200,10 @@ class PagedCache:
         n = k_draft.shape[1]
         self._rows(k_draft, "k_draft", n, self.H)
         self._rows(v_draft, "v_draft", n, self.H)
+        if path is not None:
+            self._each(path, "path", path.shape[-1])
+        self._each(path_lens, "path_lens")
+        self._each(pos, "pos")
         K.kvarn_commit_tokens(self.cfg, k_draft, v_draft, n, path, min(n, T) if path is None else path.shape[1],
                               path_lens, pos, self.table, self.max_blocks, self.w.batch, self.tail, self.pool,
                               self.err, stream)
@@ -208,17 +222,22 @@ class PagedCache:
 
     def alloc(self, tile_begin, tile_end, stream=None):
         """Give the open entries of tiles [tile_begin[b], tile_end[b]) free blocks."""
+        self._each(tile_begin, "tile_begin")
+        self._each(tile_end, "tile_end")
         need = K.kvarn_pages_workspace_bytes(self.cfg, self.w.batch)
         K.kvarn_alloc_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, tile_begin, tile_end,
                              self._refs(stream), self._workspace("pages", need, stream), need, self.err, stream)
 
     def free(self, tile_begin, tile_end, stream=None):
         """Release the blocks of tiles [tile_begin[b], tile_end[b])."""
+        self._each(tile_begin, "tile_begin")
+        self._each(tile_end, "tile_end")
         K.kvarn_free_blocks(self.cfg, self.table, self.max_blocks, self.w.batch, tile_begin, tile_end,
                             self._refs(stream), self.err, stream)
 
     def free_behind_window(self, lens, window, n_sinks=0, stream=None):
         """Release the tiles that no query at position lens[b] - 1 or later sees."""
+        self._each(lens, "lens")
         with self._on(stream):  # the ranges are written, and their memory reused, in the order of the call's stream
             begin = torch.full_like(lens, min(-(-n_sinks // T), self.max_blocks))
             end = ((lens - window).clamp_min(0) // T).to(torch.int32)
@@ -228,7 +247,8 @@ class PagedCache:
     def fork(self, parent, group, lens=None, stream=None):
         """Slot b takes the sequence of slot parent[b] (within its group of
         `group` slots; -1 empties it): open tiles, table rows, counts, lens."""
-        lens = self.lens if lens is None else lens
+        self._each(parent, "parent")
+        lens = self._each(self.lens if lens is None else lens, "lens")
         refs = self._refs(stream)
         K.kvarn_fork_tails(self.cfg, parent, group, self.w.batch, lens, self.max_blocks, self.tail, self.err, stream)
         K.kvarn_fork_sequences(self.cfg, parent, group, self.w.batch, self.table, self.max_blocks, lens, refs,

@@ -277,3 +277,33 @@ def test_every_tensor_has_to_lie_on_the_current_device(name, monkeypatch):
                 call(BAD, *args[:i], Elsewhere(), *args[i + 1:], stream=0, check=False)
     monkeypatch.setattr(K, "_here", lambda: 1, raising=False)
     assert call(BAD, *(Elsewhere() if x == 16 else x for x in args), stream=0, check=False) == UNS
+
+
+def test_index_arrays_have_an_entry_per_sequence(monkeypatch):
+    """A shorter array would be read past its end on the device."""
+    for name in K.EXPORTS:
+        if not name.endswith("_bytes"):
+            monkeypatch.setattr(K, name, lambda *a, **kw: 0)
+    c = PagedCache(I.Workload("short", 3, 8, 2, "f16", [300, 200, 1], seed=1, max_tokens=301), "cpu")
+    q, kv = torch.zeros(3, 4, 8, 128, dtype=torch.float16), torch.zeros(3, 4, 2, 128, dtype=torch.float16)
+    mask, path = torch.zeros(3, 4, 1, dtype=torch.int64), torch.zeros(3, 2, dtype=torch.int32)
+    good = torch.zeros(3, dtype=torch.int32)
+    calls = {
+        "lens": [lambda x: c.window(q, 4, q, 100, lens=x), lambda x: c.tree(q, kv, kv, mask, q, lens=x),
+                 lambda x: c.fork(good, 3, lens=x), lambda x: c.free_behind_window(x, 100)],
+        "counts": [lambda x: c.tree(q, kv, kv, mask, q, counts=x)],
+        "path_lens": [lambda x: c.commit(kv, kv, path, x, good)],
+        "pos": [lambda x: c.commit(kv, kv, None, good, x)],
+        "tile_begin": [lambda x: c.alloc(x, good), lambda x: c.free(x, good)],
+        "tile_end": [lambda x: c.alloc(good, x), lambda x: c.free(good, x)],
+        "parent": [lambda x: c.fork(x, 3)],
+    }
+    for name, each in calls.items():
+        for call in each:
+            call(good)
+            for bad in (good[:2], torch.zeros(4, dtype=torch.int32), torch.zeros((), dtype=torch.int32)):
+                with pytest.raises(ValueError, match=name):
+                    call(bad)
+    c.commit(kv, kv, path, good, good)
+    with pytest.raises(ValueError, match="path"):
+        c.commit(kv, kv, path[:2], good, good)
