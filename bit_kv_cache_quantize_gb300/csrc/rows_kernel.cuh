@@ -405,8 +405,9 @@ __global__ void __launch_bounds__(RAW_THREADS, 2) raw_rows_kernel(MQParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         s[e] = quad_sum(s[e]) * sl2;
-        if (sees(e, t)) {  // (a weight of 0 counts: 0 times an infinity is NaN)
-          const float w = ex2_ftz(s[e] - m_run[e]);
+        // (a weight of 0 counts: 0 times an infinity is NaN; a NaN has spoilt the row already)
+        const float w = sees(e, t) ? ex2_ftz(s[e] - m_run[e]) : -1.f;
+        if (w >= 0.f) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
 #pragma unroll
