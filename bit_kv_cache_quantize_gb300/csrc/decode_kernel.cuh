@@ -131,11 +131,13 @@ __device__ void tail_chunk(const DecodeParams& p, int b, int h, int len, unsigne
 // (WIN_SPLIT) or as one more CTA of a cluster that merges its own partials
 // (WIN_CLUSTER, small calls).
 constexpr int WIN_NONE = 0, WIN_SPLIT = 1, WIN_CLUSTER = 2;
+template <int WIN>
+using DecParams = std::conditional_t<WIN == WIN_NONE, DecodeParams, WindowParams>;
 template <typename E, int NW>
-__device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, const WinTiles& wt, unsigned char* smem,
+__device__ void win_tail_chunk(const WindowParams& p, int b, int h, int len, const WinTiles& wt, unsigned char* smem,
                                float* part, int64_t part_stride);
 template <int NW, typename O>
-__device__ void win_cluster_merge(const DecodeParams& p, int b, int h, const float* part, O* out);
+__device__ void win_cluster_merge(const WindowParams& p, int b, int h, const float* part, O* out);
 
 // Unpacking codes to exact fp16 operands.  A code field ORed into the
 // mantissa of 1024.0 (0x6400) and 1024 subtracted gives the code exactly.
@@ -177,7 +179,7 @@ __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
 // WIN: the chunks walk the tiles of win_tiles() and the tiles a window or the
 // first tokens end in are masked; each has at least one visible token.
 template <typename E, int KBITS, int VBITS, int NW, int WIN, typename O = float>
-__global__ void __launch_bounds__(32 * NW, 2) decode_packed_kernel(DecodeParams p, O* __restrict__ out = nullptr) {
+__global__ void __launch_bounds__(32 * NW, 2) decode_packed_kernel(DecParams<WIN> p, O* __restrict__ out = nullptr) {
   using KL = KeyLayout<KBITS>;
   constexpr int KREC = rec_bytes(KBITS), KROW = D * KBITS / 8;  // KROW: code bytes per token
   constexpr int VREC = rec_bytes(VBITS);
@@ -628,7 +630,7 @@ __device__ void tail_chunk(const DecodeParams& p, int b, int h, int len, unsigne
 // the inverse rotation to the packed-tile part, add the raw part, normalise.
 // O: float, or a 16-bit type (one rounding of the fp32 result).
 template <bool WIN, typename O>
-__global__ void __launch_bounds__(128) combine_kernel(DecodeParams p, int rotate, int batch, O* __restrict__ out) {
+__global__ void __launch_bounds__(128) combine_kernel(DecParams<WIN ? WIN_SPLIT : WIN_NONE> p, int rotate, int batch, O* __restrict__ out) {
   wait_prerequisite();  // the split-K kernel's partials
   const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (wid >= batch * p.num_q_heads) return;

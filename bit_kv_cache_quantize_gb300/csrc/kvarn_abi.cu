@@ -367,16 +367,16 @@ kvarn_status kvarn_window_attention(const kvarn_config* cfg, const void* q, int3
   const auto pool = static_cast<const unsigned char*>(block_pool);
   const bool out16 = out_dtype == KVARN_OUT_16;
   if (n_queries == 1) {
-    DecodeParams p{q, block_table, seq_lens, pool, tail_pool, static_cast<float*>(workspace), dev_err,
+    WindowParams p{{q, block_table, seq_lens, pool, tail_pool, static_cast<float*>(workspace), dev_err,
                    static_cast<int64_t>(kvarn_block_bytes(cfg)), softmax_scale, max_blocks, cfg->num_kv_heads,
                    cfg->num_q_heads, G, cfg->num_blocks, w.chunk, w.n_chunks, cfg->k_bits, cfg->v_bits, 0, 0,
-                   static_cast<int64_t>(workspace_bytes), w.window, w.n_sinks, batch, w.cluster};
+                   static_cast<int64_t>(workspace_bytes)}, w.window, w.n_sinks, batch, w.cluster};
     return cuda_status(launch_window_decode(p, cfg->dtype, batch, out, out16, static_cast<cudaStream_t>(stream)));
   }
-  MQParams p{q, block_table, seq_lens, pool, tail_pool, static_cast<float*>(workspace), dev_err,
+  RowsParams p{{q, block_table, seq_lens, pool, tail_pool, static_cast<float*>(workspace), dev_err,
              static_cast<int64_t>(kvarn_block_bytes(cfg)), softmax_scale, max_blocks, cfg->num_kv_heads,
              cfg->num_q_heads, G, cfg->num_blocks, n_queries, w.n_rb, w.chunk, w.n_chunks, cfg->k_bits, cfg->v_bits,
-             static_cast<int64_t>(workspace_bytes), w.window, w.n_sinks};
+             static_cast<int64_t>(workspace_bytes)}, w.window, w.n_sinks};
   return cuda_status(launch_window_multiquery(p, cfg->dtype, batch, out, out16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -424,10 +424,10 @@ kvarn_status kvarn_tree_attention(const kvarn_config* cfg, const void* q, const 
       !aligned16(out) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
     return KVARN_ERR_INVALID;
   if (workspace_bytes < t.ws_bytes) return KVARN_ERR_INVALID;
-  MQParams p{q, block_table, seq_lens, static_cast<const unsigned char*>(block_pool), tail_pool,
+  RowsParams p{{q, block_table, seq_lens, static_cast<const unsigned char*>(block_pool), tail_pool,
              static_cast<float*>(workspace), dev_err, static_cast<int64_t>(kvarn_block_bytes(cfg)), softmax_scale,
              max_blocks, cfg->num_kv_heads, cfg->num_q_heads, cfg->num_q_heads / cfg->num_kv_heads, cfg->num_blocks,
-             n_nodes, t.n_rb, t.chunk, t.n_chunks, cfg->k_bits, cfg->v_bits, static_cast<int64_t>(workspace_bytes),
+             n_nodes, t.n_rb, t.chunk, t.n_chunks, cfg->k_bits, cfg->v_bits, static_cast<int64_t>(workspace_bytes)},
              0, 0, k_draft, v_draft, tree_mask, node_counts};
   return cuda_status(launch_tree(p, cfg->dtype, batch, out, out_dtype == KVARN_OUT_16,
                                  static_cast<cudaStream_t>(stream)));

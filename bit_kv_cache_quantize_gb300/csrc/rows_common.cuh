@@ -45,6 +45,8 @@ namespace {
 // of those the first n_sinks and the last `window`; or, for a node of a
 // drafted tree, every cached token and the nodes its mask row names.
 constexpr int MQ_CAUSAL = 0, MQ_WINDOW = 1, MQ_TREE = 2;
+template <int MODE>
+using ModeParams = std::conditional_t<MODE == MQ_CAUSAL, MQParams, RowsParams>;
 
 constexpr float MQ_LOG2E = 1.4426950408889634f;
 constexpr uint32_t MAGIC_F16 = 0x64006400u;  // 1024.0 in both fp16 halves
@@ -124,8 +126,10 @@ __device__ __forceinline__ float* mq_part(const MQParams& p, int b, int h, int r
 
 // Query tokens of sequence b (a tree may have fewer nodes than the array).
 template <int MODE>
-__device__ __forceinline__ int mq_queries(const MQParams& p, int b) {
-  return MODE == MQ_TREE && p.node_counts ? p.node_counts[b] : p.n_queries;
+__device__ __forceinline__ int mq_queries(const ModeParams<MODE>& p, int b) {
+  if constexpr (MODE == MQ_TREE)
+    if (p.node_counts) return p.node_counts[b];
+  return p.n_queries;
 }
 
 // Rows of row block rb and the number of closed tiles it reads, up to the
@@ -141,7 +145,7 @@ __device__ __forceinline__ void mq_block_extent(const MQParams& p, int rb, int l
   n_need = min(len / T, pos_hi / T + 1);
 }
 // The closed tiles row block rb visits (MQ_WINDOW): from its first row's window on.
-__device__ __forceinline__ WinTiles mq_win_tiles(const MQParams& p, int rb, int len, int n_need) {
+__device__ __forceinline__ WinTiles mq_win_tiles(const RowsParams& p, int rb, int len, int n_need) {
   return win_tiles(n_need, max(0, len - p.n_queries + (rb * MQ_ROWS) / p.G + 1 - p.window), p.n_sinks);
 }
 
@@ -297,7 +301,7 @@ __device__ __forceinline__ void unpack_v(const unsigned char* vr, unsigned char*
 // partials, rotate the packed part back, add the raw part, normalise.
 // O: float, or a 16-bit type (one rounding of the fp32 result).
 template <int MODE, typename O>
-__global__ void __launch_bounds__(128) mq_combine_kernel(MQParams p, int batch, O* __restrict__ out) {
+__global__ void __launch_bounds__(128) mq_combine_kernel(ModeParams<MODE> p, int batch, O* __restrict__ out) {
   wait_prerequisite();  // the split-K kernel's partial rows
   const int wid = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int per_seq = p.n_queries * p.num_q_heads;

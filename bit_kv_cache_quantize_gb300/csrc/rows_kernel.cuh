@@ -192,7 +192,7 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x, bool& bad) {
 
 // grid (num_kv_heads * n_rowblocks, batch) x 256 threads
 template <typename E, int MODE, int PASSES>
-__global__ void __launch_bounds__(RAW_THREADS, 2) raw_rows_kernel(MQParams p) {
+__global__ void __launch_bounds__(RAW_THREADS, 2) raw_rows_kernel(RowsParams p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   allow_dependents();
   const int h = blockIdx.x / p.n_rowblocks, rb = blockIdx.x % p.n_rowblocks, b = blockIdx.y;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(RAW_THREADS, 2) raw_rows_kernel(MQParams p) {
 // grid (n_chunks, num_kv_heads * n_rowblocks, batch) x 512 threads.  With
 // n_chunks == 1 the CTA writes the result rows, else partial rows.
 template <typename E, int KBITS, int VBITS, int MODE, int PASSES, typename O>
-__global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(MQParams p, O* __restrict__ out) {
+__global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(RowsParams p, O* __restrict__ out) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   allow_dependents();
   const int chunk = blockIdx.x, h = blockIdx.y / p.n_rowblocks, rb = blockIdx.y % p.n_rowblocks, b = blockIdx.z;
@@ -1188,7 +1188,7 @@ __global__ void __launch_bounds__(RQ_THREADS, 1) rows_kernel(MQParams p, O* __re
 }
 
 template <typename E, int KBITS, int VBITS, int MODE, typename O>
-cudaError_t launch_rows_t(const MQParams& p, int batch, O* out, cudaStream_t s) {
+cudaError_t launch_rows_t(const RowsParams& p, int batch, O* out, cudaStream_t s) {
   constexpr int PASSES = std::is_same<E, __nv_bfloat16>::value && std::is_same<O, __nv_bfloat16>::value ? 1 : 2;
   const size_t raw_smem = sizeof(RawSmem) + 128, smem = sizeof(RQSmem) + 128;
   static std::atomic<uint64_t> raw_done{0}, attr_done{0};
@@ -1208,7 +1208,7 @@ cudaError_t launch_rows_t(const MQParams& p, int batch, O* out, cudaStream_t s) 
 }
 
 template <int MODE, typename E, typename O>
-cudaError_t launch_rows(const MQParams& p, int batch, O* out, cudaStream_t s) {
+cudaError_t launch_rows(const RowsParams& p, int batch, O* out, cudaStream_t s) {
   if (p.k_bits == 2) return launch_rows_t<E, 2, 2, MODE>(p, batch, out, s);
   return p.v_bits == 4 ? launch_rows_t<E, 4, 4, MODE>(p, batch, out, s) : launch_rows_t<E, 4, 2, MODE>(p, batch, out, s);
 }

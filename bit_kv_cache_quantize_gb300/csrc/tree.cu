@@ -15,7 +15,7 @@
 
 namespace kvarn {
 
-cudaError_t launch_tree(const MQParams& p, int dtype, int batch, void* out, bool out16, cudaStream_t s) {
+cudaError_t launch_tree(const RowsParams& p, int dtype, int batch, void* out, bool out16, cudaStream_t s) {
   if (dtype == KVARN_DTYPE_BF16)
     return out16 ? launch_rows<MQ_TREE, __nv_bfloat16>(p, batch, static_cast<__nv_bfloat16*>(out), s)
                  : launch_rows<MQ_TREE, __nv_bfloat16>(p, batch, static_cast<float*>(out), s);

@@ -29,7 +29,7 @@ namespace kvarn {
 // not finite it takes such values out, repeats the product and adds them by
 // their whole weights (the test of the sums costs 64 operations a thread).
 template <typename E, int NW>
-__device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, const WinTiles& wt, unsigned char* smem,
+__device__ void win_tail_chunk(const WindowParams& p, int b, int h, int len, const WinTiles& wt, unsigned char* smem,
                                float* part, int64_t part_stride) {
   const int n = len % T;
   constexpr int NB = 8 / NW;  // 16-token blocks per warp
@@ -190,7 +190,7 @@ __device__ void win_tail_chunk(const DecodeParams& p, int b, int h, int len, con
 // its whole latency (39 us of 356 at 256 ragged sequences); here four share an
 // SM, and the packed tiles start under them.
 template <typename E>
-__global__ void __launch_bounds__(128, 4) win_tail_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(128, 4) win_tail_kernel(WindowParams p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   allow_dependents();
   const int h = blockIdx.x, b = blockIdx.y, len = p.seq_lens[b];
@@ -230,7 +230,7 @@ __device__ __forceinline__ void cluster_sync_all() {
 // shared memory and writes the result: no workspace, no second launch (3 us of
 // a 12 us call at 8 x 4096 tokens).
 template <int NW, typename O>
-__device__ void win_cluster_merge(const DecodeParams& p, int b, int h, const float* part, O* out) {
+__device__ void win_cluster_merge(const WindowParams& p, int b, int h, const float* part, O* out) {
   const int n = p.n_chunks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cluster_sync_all();
   const int g = blockIdx.x * NW + warp;  // the cluster spans the grid's x: blockIdx.x is the rank
@@ -266,7 +266,7 @@ __device__ void win_cluster_merge(const DecodeParams& p, int b, int h, const flo
 
 namespace {
 template <typename E, int KBITS, int VBITS, typename O>
-cudaError_t launch_window_cluster_t(const DecodeParams& p, int batch, O* out, cudaStream_t s) {
+cudaError_t launch_window_cluster_t(const WindowParams& p, int batch, O* out, cudaStream_t s) {
   auto kernel = decode_packed_kernel<E, KBITS, VBITS, 4, WIN_CLUSTER, O>;
   const size_t smem = sizeof(DecSmem<KBITS, VBITS, 4>) + 128;
   static std::atomic<uint64_t> attr_done{0};
@@ -287,7 +287,7 @@ cudaError_t launch_window_cluster_t(const DecodeParams& p, int batch, O* out, cu
 }
 
 template <typename E, int KBITS, int VBITS, int NW, typename O>
-cudaError_t launch_window_decode_t(const DecodeParams& p, int batch, O* out, cudaStream_t s) {
+cudaError_t launch_window_decode_t(const WindowParams& p, int batch, O* out, cudaStream_t s) {
   const size_t smem = sizeof(DecSmem<KBITS, VBITS, NW>) + 128;
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = smem_attr_once(attr_done, (const void*)decode_packed_kernel<E, KBITS, VBITS, NW, WIN_SPLIT>, (int)smem);
@@ -303,7 +303,7 @@ cudaError_t launch_window_decode_t(const DecodeParams& p, int batch, O* out, cud
 }
 
 template <typename E, typename O>
-cudaError_t launch_window_decode_p(const DecodeParams& p, int batch, O* out, cudaStream_t s) {
+cudaError_t launch_window_decode_p(const WindowParams& p, int batch, O* out, cudaStream_t s) {
   static_assert(sizeof(DecSmem<2, 2, 4>) >= 8 * 16 * D * 2 && sizeof(DecSmem<2, 2, 4>) >= sizeof(DecMerge<4>) &&
                     sizeof(DecSmem<2, 2, 8>) >= sizeof(DecMerge<8>),
                 "the open tile's buffers fit");
@@ -322,7 +322,7 @@ cudaError_t launch_window_decode_p(const DecodeParams& p, int batch, O* out, cud
 }
 }  // namespace
 
-cudaError_t launch_window_decode(const DecodeParams& p, int dtype, int batch, void* out, bool out16, cudaStream_t s) {
+cudaError_t launch_window_decode(const WindowParams& p, int dtype, int batch, void* out, bool out16, cudaStream_t s) {
   if (dtype == KVARN_DTYPE_BF16)
     return out16 ? launch_window_decode_p<__nv_bfloat16>(p, batch, static_cast<__nv_bfloat16*>(out), s)
                  : launch_window_decode_p<__nv_bfloat16>(p, batch, static_cast<float*>(out), s);
@@ -330,7 +330,7 @@ cudaError_t launch_window_decode(const DecodeParams& p, int dtype, int batch, vo
                : launch_window_decode_p<__half>(p, batch, static_cast<float*>(out), s);
 }
 
-cudaError_t launch_window_multiquery(const MQParams& p, int dtype, int batch, void* out, bool out16, cudaStream_t s) {
+cudaError_t launch_window_multiquery(const RowsParams& p, int dtype, int batch, void* out, bool out16, cudaStream_t s) {
   if (dtype == KVARN_DTYPE_BF16)
     return out16 ? launch_rows<MQ_WINDOW, __nv_bfloat16>(p, batch, static_cast<__nv_bfloat16*>(out), s)
                  : launch_rows<MQ_WINDOW, __nv_bfloat16>(p, batch, static_cast<float*>(out), s);
