@@ -106,9 +106,15 @@ typedef enum kvarn_dtype {
 /* Type of an attention result (the calls that take out_dtype).  KVARN_OUT_16
  * is for a caller whose next layer takes 16 bits: the fp32 result rounded once.
  * For bfloat16 and several query rows (a window chunk, a tree) the products
- * also take their operands at one rounding each, which adds at most about as
- * much again: half a bfloat16 step per weight, averaged over the tokens, and a
- * float16 half step per query channel. */
+ * also take their operands at one rounding each.  A weight is off by up to half
+ * a bfloat16 step, 2^-8 of itself (over many tokens such errors average out).
+ * A rotated query channel is off by up to half a float16 step, 2^-11 of itself,
+ * which moves a score by up to 2^-11 sum_c |q_c k_c| softmax_scale and its
+ * weight by as much, relative: this part grows with the scores, and is an
+ * eighth of what the query's own rounding to bfloat16 may have done.  At scores
+ * of a few units a result is 0.0020 of the results' rms off, of which the
+ * result's own rounding is 0.0017.  KVARN_OUT_F32 keeps both operands in two
+ * parts. */
 typedef enum kvarn_out_dtype {
   KVARN_OUT_F32 = 0, /* float32 */
   KVARN_OUT_16 = 1   /* cfg->dtype */
