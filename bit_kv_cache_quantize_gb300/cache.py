@@ -241,6 +241,8 @@ class PagedCache:
     def free_behind_window(self, lens, window, n_sinks=0, stream=None):
         """Release the tiles that no query at position lens[b] - 1 or later sees."""
         self._each(lens, "lens")
+        if window < 1 or n_sinks < 0:  # (as the window attention: such a range would reach tiles that are in use)
+            raise ValueError(f"window >= 1 and n_sinks >= 0, got {window} and {n_sinks}")
         with self._on(stream):  # the ranges are written, and their memory reused, in the order of the call's stream
             begin = torch.full_like(lens, min(-(-n_sinks // T), self.max_blocks))
             end = ((lens - window).clamp_min(0) // T).to(torch.int32)

@@ -40,7 +40,7 @@
  *
  * Packed format (one record per tile x KV head, 16-byte aligned):
  *   K record 8704 B: g[128] FP8 E4M3 per-channel scale | a[128] FP8 E4M3
- *     per-token step | b[128] FP16 (little-endian) per-token zero-point |
+ *     per-token step (2^-9 or more: never 0) | b[128] FP16 (little-endian) per-token zero-point |
  *     codes[128 tokens][64 B], byte i of token t = code[t][2i] |
  *     code[t][2i+1] << 4.
  *   V record 4608 B: same 512-byte header | codes[128 channels][32 B]:

@@ -307,3 +307,12 @@ def test_index_arrays_have_an_entry_per_sequence(monkeypatch):
     c.commit(kv, kv, path, good, good)
     with pytest.raises(ValueError, match="path"):
         c.commit(kv, kv, path[:2], good, good)
+
+
+@pytest.mark.parametrize("window,n_sinks", [(0, 0), (-300, 0), (100, -1)])
+def test_no_release_behind_an_impossible_window(window, n_sinks, monkeypatch):
+    monkeypatch.setattr(K, "kvarn_free_blocks", lambda *a, **kw: 0)
+    c = PagedCache(I.Workload("behind", 2, 8, 2, "f16", [300, 200], seed=1, max_tokens=301), "cpu")
+    c.free_behind_window(c.lens, 100, 0)
+    with pytest.raises(ValueError, match="window >= 1"):
+        c.free_behind_window(c.lens, window, n_sinks)
